@@ -845,9 +845,13 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          // neither 0 nor infinite: a masked score, -infinity, stays one, and a
-          // score of 0 stays 0
-          const float f = fminf(fmaxf(sc[nt][k] * ks, 1.17549435e-38f), 1.2676506e30f);  // 2^-126, 2^100
+          // Neither 0 nor so large that a product with a sum (below 2^17) leaves
+          // the range: a masked score, -infinity, stays one, a score of 0 stays
+          // 0, and no other becomes infinite.  Every score is rounded by
+          // itself, as the maximum is: with the exact product in its place the
+          // largest one's distance from the maximum would be that rounding,
+          // 2^5 and more for scores of 2^29.
+          const float f = fminf(fmaxf(sc[nt][k] * ks, 1.17549435e-38f), 1.2980742e33f);  // 2^-126, 2^110
           float mx = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt)
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float m_new = fmaxf(m_run[nt][k], mx * f);
+          const float m_new = fmaxf(m_run[nt][k], __fmul_rn(mx, f));
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: every p is 0
           alpha[nt][k] = ex2_approx(m_run[nt][k] - ref);
           m_run[nt][k] = m_new;
@@ -865,7 +869,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
           for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p = ex2_approx(fmaf(s[mt][nt][2 * e + k], f, -ref));
+              const float p = ex2_approx(__fmul_rn(s[mt][nt][2 * e + k], f) - ref);
               s[mt][nt][2 * e + k] = p;
               l += p;
             }

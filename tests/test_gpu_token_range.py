@@ -1,0 +1,49 @@
+"""The token-step operators where the range of the numbers or of the bounds is wide: scores far from zero, one token
+that outweighs many small ones, elements that outweigh the rest of a vector, bounds far above the lengths."""
+import pytest
+import torch
+
+from diffusion_transformer_image_mmdit_gb300 import api
+from tests import token_oracle as T
+from tests.test_gpu_token_ops import BF16, Seqs, _gpu, device_cache, gen, random_cache, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(shape, cache, q):
+    out = torch.empty(q.shape[0], shape.H * shape.d_head, dtype=BF16, device="cuda")
+    api.mmdit_kv_attention(shape, cache, q.cuda(), out, api.alloc_workspace(api.kv_workspace_size(shape)))
+    return out.cpu()
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("tokens", [300, 8192])
+@pytest.mark.parametrize("j", [12, 17, 19, 21, 24, 52, 80])
+@pytest.mark.parametrize("q0", [1.3828125, -1.7265625])
+def test_kv_attention_scores_far_above_one(tokens, j, q0):
+    """Scores of some 2^8 2^j: the token with the largest alone is left, whatever the rounding of its score, or, where
+    two have it, their mean.  The next largest lies 2^-10 of it below (scores carry 2^-19 of the products' sum)."""
+    g = gen(j)
+    sq = Seqs(g, [tokens - 1], [1])
+    k, v, _, _ = random_cache(g, sq.n_blocks, 1, 64)
+    k, v = k & 0xB7, v & 0xB7  # finite, below 1
+    top = [sq.table[0][at // 64] for at in (70, 260)]
+    slot = [70 % 64, 260 % 64]
+    ks, vs = torch.full((sq.n_blocks, 1), 2.0 ** j), torch.ones(sq.n_blocks, 1)
+    best = torch.randint(0x40, 0x58, (64,), generator=g).to(torch.uint8) | (0x80 if q0 < 0 else 0)
+    k[top[0], 0, slot[0]] = best
+    two = tokens == 8192  # the same score once more, in another block of another scale
+    if two:
+        ks[top[1]] = 2.0 ** (j - 1)
+        k[top[1], 0] = 0
+        k[top[1], 0, slot[1]] = best + 8  # twice the value
+    cache = T.Cache(k, v, ks, vs)
+    kk, vv = cache.rows(sq.table[0], 0, tokens)
+    s = (kk * q0).sum(1)
+    first = s.sort(descending=True).values
+    assert float(first[2 if two else 1]) < float(first[0]) * (1 - 2.0 ** -10) and s[70] == first[0]
+    shape = sq.shape(2, 1, 64)
+    out = attend(shape, device_cache(k, v, ks, vs, sq), torch.full((1, 128), q0, dtype=BF16))
+    want = (vv[70] + vv[260]) / 2 if two else vv[70]
+    for h in range(2):
+        within(out.view(2, 64)[h], want, (2.0 ** -8 + 2.0 ** -18) * want.abs(), "one token")
