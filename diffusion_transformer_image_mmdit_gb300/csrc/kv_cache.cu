@@ -450,7 +450,10 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
 // largest element to [1, 2) (an element 2^-14 of that or more stays exact);
 // P is f16, so that both products have 11-bit operands and fp32 sums, and
 // the block's key scale goes to the exponent's argument, its value scale to
-// the fp32 sum of the blocks.
+// the fp32 sum of the blocks.  P's reference lies 14 below the maximum
+// (p_reference): a p stays normal, off by 2^-11 of itself at most, down to
+// 2^-28 of the largest, and by 2^-39 of the largest below, so that a token
+// which stands far above 2^28 others does not drop what they give together.
 //
 // Bound: the read of the codes, 2 d bytes per token and kv head.  Every warp
 // has its own ring of slots of one block of keys or of values, filled by bulk
@@ -568,6 +571,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t word_of(const uint4& u, int i) {
   return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
 }
+
+// The reference that p = 2^(score - reference) is taken against, from a maximum:
+// p reaches kPTop = 2^14, of f16's 65504.  Where the fp32 steps of the scores
+// are so coarse that 14 could round to more, the maximum itself; any reference
+// serves, since a row's sum l and its output go by the same one.  The output is
+// kept in units of kPTop (kPUnit rides on the blocks' value scales), so that it
+// has the range of the values.
+constexpr float kPTop = 16384.0f, kPUnit = 1.0f / 16384.0f;
+__device__ __forceinline__ float p_reference(float m) { return fabsf(m) < 1048576.0f ? m - 14.0f : m; }
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a) {
@@ -796,7 +808,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
       const int j = j0 + warp + kKvWarps * i;
       const bool lost = __shfl_sync(0xffffffffu, id_w, i & 31) < 0;
       const float ks = __shfl_sync(0xffffffffu, ks_w, i & 31);
-      const float vs = __shfl_sync(0xffffffffu, vs_w, i & 31);
+      const float vs = __shfl_sync(0xffffffffu, vs_w, i & 31) * kPUnit;
       const bool edge = j * kBlk + kBlk > lim_lo || lost;  // some row does not see all of the block's keys
 
       const uint8_t* kt = wait_item();
@@ -860,7 +872,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float m_new = fmaxf(m_run[nt][k], __fmul_rn(mx, f));
+          const float m_new = fmaxf(m_run[nt][k], p_reference(__fmul_rn(mx, f)));
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: every p is 0
           alpha[nt][k] = ex2_approx(m_run[nt][k] - ref);
           m_run[nt][k] = m_new;
@@ -1017,7 +1029,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
         l = fmaf(f, sh_l[w][row], l), v0 = fmaf(f, t.x, v0), v1 = fmaf(f, t.y, v1);
       }
       if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that sees no key: zeros
+        const float inv = l == 0.f ? 0.f : kPTop / l;  // a row that sees no key: zeros
         const int t = (r0 + row) / d.G, hq = r0 + row - t * d.G;
         *reinterpret_cast<uint32_t*>(a.out + ((long long)(sq.s0 + t) * d.H + (long long)h * d.G + hq) * HD + ch) =
             pack_bf16x2(v0 * inv, v1 * inv);
@@ -1128,7 +1140,7 @@ __global__ void __launch_bounds__(W * 32) kv_combine_kernel(const KvAttnArgs a, 
       const float f = ex2_approx(sh_ml[w].x - ref);
       ll = fmaf(f, sh_ml[w].y, ll), v0 = fmaf(f, sh_o[w][ch], v0), v1 = fmaf(f, sh_o[w][ch + 1], v1);
     }
-    const float inv = ll == 0.f ? 0.f : 1.0f / ll;
+    const float inv = ll == 0.f ? 0.f : kPTop / ll;
     *reinterpret_cast<uint32_t*>(out + ch) = pack_bf16x2(v0 * inv, v1 * inv);
   }
 }

@@ -16,6 +16,11 @@ def attend(shape, cache, q):
     return out.cpu()
 
 
+def value_codes(v):
+    """[..., d, 64] codes of values [..., 64, d]."""
+    return T.e4m3(v).transpose(-1, -2).contiguous()
+
+
 # ------------------------------------------------------------------ attention
 @pytest.mark.parametrize("tokens", [300, 8192])
 @pytest.mark.parametrize("j", [12, 17, 19, 21, 24, 52, 80])
@@ -47,3 +52,28 @@ def test_kv_attention_scores_far_above_one(tokens, j, q0):
     want = (vv[70] + vv[260]) / 2 if two else vv[70]
     for h in range(2):
         within(out.view(2, 64)[h], want, (2.0 ** -8 + 2.0 ** -18) * want.abs(), "one token")
+
+
+@pytest.mark.parametrize("tokens", [300, 8192, 65537])
+@pytest.mark.parametrize("nats", [12, 16, 18, 22])
+@pytest.mark.parametrize("d", [64, 128])
+def test_kv_attention_one_token_above_many(tokens, nats, d):
+    """One token (its value 0) stands `nats` above all others, which share the rest: what they give is the output.  P is
+    rounded to f16, half a step 2^-11, or 2^-39 of the largest p where that is more; scores carry 2^-19 of their
+    magnitude and P's sums 2^-18; the output is rounded to bf16, 2^-8."""
+    g = gen(nats)
+    sq = Seqs(g, [tokens - 1], [1])
+    code = int(T.e4m3(torch.tensor([-2.0 * nats]))[0])
+    assert float(T.e4m3_value(torch.tensor([code], dtype=torch.uint8))) == -2 * nats
+    k = torch.full((sq.n_blocks, 1, 64, d), code, dtype=torch.uint8)
+    v = value_codes(1 + torch.rand(sq.n_blocks, 1, 64, d, generator=g))
+    blk = sq.table[0][1]
+    k[blk, 0, 5], v[blk, 0, :, 5] = 0, 0
+    ks, vs = torch.full((sq.n_blocks, 1), 0.5), torch.ones(sq.n_blocks, 1)
+    out = attend(sq.shape(4, 1, d, scale=1.0 / d), device_cache(k, v, ks, vs, sq), torch.ones(1, 4 * d, dtype=BF16))
+    kk, vv = T.Cache(k, v, ks, vs).rows(sq.table[0], 0, tokens)
+    p = torch.softmax(kk.mean(1), 0)
+    o = p @ vv
+    tol = 2.0 ** -8 * o + (2.0 ** -11 + 2.0 ** -18 + nats * 2.0 ** -19) * 1.01 * o + tokens * 2.0 ** -39 * 2 * p.max()
+    for h in range(4):
+        within(out.view(4, d)[h], o, tol, "the many")
