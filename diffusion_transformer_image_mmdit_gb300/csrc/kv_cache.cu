@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
 // operand of m16n8k16 and the query rows its 8-column operand, so up to 8
 // rows (one token of a group of up to 8 heads) waste nothing.  The codes
 // become f16 (exact); q is f16 after a power of two per row has brought its
-// largest element to [1, 2) (an element 2^-14 of that or more stays exact);
+// largest element to [2^14, 2^15) (an element of 2^-31 of that stays exact);
 // P is f16, so that both products have 11-bit operands and fp32 sums, and
 // the block's key scale goes to the exponent's argument, its value scale to
 // the fp32 sum of the blocks.  P's reference lies 14 below the maximum
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
       for (int i = 0; i < HD / 4; ++i) mx = fmaxf(mx, finite_abs(x8[i]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = mx > 0.f ? max(-126, min(126, (int)(__float_as_uint(mx) >> 23) - 127)) : 0;
+      const int e = mx > 0.f ? max(-112, min(127, (int)(__float_as_uint(mx) >> 23) - 127)) - 14 : 0;
       const float down = exp2_int(-e);
 #pragma unroll
       for (int i = 0; i < HD / 16; ++i) {
@@ -857,13 +857,13 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          // Neither 0 nor so large that a product with a sum (below 2^17) leaves
+          // Neither 0 nor so large that a product with a sum (below 2^32) leaves
           // the range: a masked score, -infinity, stays one, a score of 0 stays
           // 0, and no other becomes infinite.  Every score is rounded by
           // itself, as the maximum is: with the exact product in its place the
           // largest one's distance from the maximum would be that rounding,
           // 2^5 and more for scores of 2^29.
-          const float f = fminf(fmaxf(sc[nt][k] * ks, 1.17549435e-38f), 1.2980742e33f);  // 2^-126, 2^110
+          const float f = fminf(fmaxf(sc[nt][k] * ks, 1.17549435e-38f), 3.9614081e28f);  // 2^-126, 2^95
           float mx = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt)

@@ -5,7 +5,8 @@ import torch
 
 from diffusion_transformer_image_mmdit_gb300 import api
 from tests import token_oracle as T
-from tests.test_gpu_token_ops import BF16, Seqs, _gpu, device_cache, gen, random_cache, within  # noqa: F401
+from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn,
+                                      within)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,22 @@ def test_kv_attention_one_token_above_many(tokens, nats, d):
     tol = 2.0 ** -8 * o + (2.0 ** -11 + 2.0 ** -18 + nats * 2.0 ** -19) * 1.01 * o + tokens * 2.0 ** -39 * 2 * p.max()
     for h in range(4):
         within(out.view(4, d)[h], o, tol, "the many")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_kv_attention_query_channel_that_meets_zero_keys(d):
+    """A channel of the queries 2^20 above the others, whose keys are 0, takes nothing from the others' products."""
+    g = gen(d)
+    sq = Seqs(g, [255], [1])
+    k, v = T.e4m3(randn(g, sq.n_blocks, 1, 64, d)), T.e4m3(randn(g, sq.n_blocks, 1, d, 64))
+    k[..., 9] = 0
+    ks = vs = torch.ones(sq.n_blocks, 1)
+    q = randn(g, 1, 2 * d).to(BF16)
+    q.view(2, d)[:, 9] = 2.0 ** 20
+    out = attend(sq.shape(2, 1, d), device_cache(k, v, ks, vs, sq), q)
+    kk, vv = T.Cache(k, v, ks, vs).rows(sq.table[0], 0, 256)
+    qq = q.view(2, d).to(F64)
+    p = torch.softmax(qq @ kk.t() * d ** -0.5, 1)
+    o, mag = p @ vv, (qq.abs() @ kk.abs().t() * d ** -0.5).amax(1, keepdim=True)
+    tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2.0 ** -18 + mag * 2.0 ** -19) * 1.01 * (p @ vv.abs()) + 256 * 2.0 ** -39 * vv.abs().amax()
+    within(out.view(2, d), o, tol, "outlier channel")
