@@ -7,8 +7,6 @@
 #include <atomic>
 #include <mutex>
 
-#include <cuda_fp16.h>
-
 #include "capi_util.h"
 #include "mmdit.h"
 #include "mmdit_internal.h"
@@ -270,33 +268,30 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const void* __restrict
 
 // y[b, n] = sum over groups of s[n, group] * (sum_k q[n, k] x[b, k]) + bias.
 //
-// A code n = q + 8 (0 .. 15) in the low bits of a 16-bit half, read as f16, is
-// the subnormal n 2^-24, and four bits further up 16 n 2^-24.  So one mask
-// makes two codes of a word an operand of the f16 matrix instruction
-// (m16n8k16, 16 rows of W), and a word of eight takes four masks and a shift;
-// the 16 is taken out of the elements of x that meet those codes, and the 8
-// off a group's sum,
-//   sum_k q x = 2^24 sum_k (n 2^-24) x - 8 sum_k x,
-// by starting it at the second term, formed once per block in fp32.  x is f16
-// after a power of two 2^-e that brings the largest of an item's 512 elements
-// to [2^14, 2^15): the eight significant bits of a bf16 value stay exact down
-// to 2^-26 of that element, and are off by at most 2^-35 of it below.  The sums
-// of a group are fp32 (the matrix unit cuts off where an addition would round:
-// the largest relative error of a result is some 1e-6 where one element
-// outweighs the rest of x, 5e-7 in general) and are scaled and added up in
-// fp32.  (The e4m3 instruction would take a mask per four codes, but it runs
-// as conversions and f16 products here: 40 instructions for one.)
+// Both operands of the matrix instruction (m16n8k16, 16 rows of W) are bf16 and
+// exact: x as it is given, and the codes as q 2^-6.  A code n = q + 8 (0 .. 15)
+// in the low bits of a 16-bit half, read as bf16, is the subnormal n 2^-133, and
+// four bits further up n 2^-129 (the first normal numbers go on where the
+// subnormal ones end), so a mask and one fused multiply-add for two codes,
+//   n 2^-133 2^127 - 2^-3 = n 2^-129 2^123 - 2^-3 = q 2^-6,
+// make them; a word of eight takes four of each and a shift.  The sums of a
+// group are fp32 (the matrix unit cuts off where an addition would round) and
+// are scaled and added up in fp32; what is summed is q x itself, so a term whose
+// code is 0 takes nothing from the others, however large its x, and an infinity
+// gives what the definition does.  (Codes left at n, with 8 sum x taken off
+// again, saved the multiply-adds, but cost the results the bits of 8 sum |x|.
+// The e4m3 instruction would take a mask per four codes, but it runs as
+// conversions and f16 products here: 40 instructions for one.)
 //
 // The bound is the read of the codes, then instruction issue: an item of 16
 // rows and 4 chunks (4 KB) is due every 180 cycles of an SM at full bandwidth,
-// and takes some 450 instructions with up to 8 vectors, 700 with more and
-// groups of 32, besides 160 cycles of the L1 data path (the operands from
-// shared memory, and 8 cycles for a load of 8 rows).  So each warp streams its own items straight into registers,
-// each chunk's loads for the next item issued as soon as the chunk has been
+// and takes some 540 instructions with up to 8 vectors, besides 150 cycles of
+// the L1 data path (the operands from shared memory, and 8 cycles for a load of
+// 8 rows).  So each warp streams its own items straight into registers, each
+// chunk's loads for the next item issued as soon as the chunk has been
 // multiplied, across tiles, with no barrier in between; x stays in shared
 // memory for all tiles of a block, one block of 16 warps per SM, since staging
-// it costs every block the same reads of L2 (two blocks of 8: 13 vectors, 4096
-// rows of 12288 24.4 us, one of 16 20.5).  The warps of a block form teams:
+// it costs every block the same reads of L2.  The warps of a block form teams:
 // a team takes a tile of 16 rows (SwiGLU: 8 gate rows and their 8 up rows), its
 // warps split the tile's items, leave their parts in shared memory, and one of
 // them in turn adds the parts up a tile later, so no warp waits for the slowest
@@ -306,12 +301,12 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const void* __restrict
 // cluster of blocks splits K and adds the parts up through distributed shared
 // memory.
 //
-// Measured: 131071 rows of 4096, groups of 64, three vectors 51.7 us (286 MB,
-// 5.5 TB/s, 0.82 of the copy bandwidth; 49 % of the issue slots, 67 % of the L1
-// data path); 24576 rows (SwiGLU), one vector 14.4 us (3.6 TB/s: 4 us of it are
-// launch, staging and the last tiles); 4096 x 4096, one vector 4.8 us; 4096 x
-// 12288, groups of 32, 13 vectors 16.5 us: 5 for staging, 8 for three items per
-// warp (42 % of the issue slots), 2 for the exchange.
+// Measured: 131071 rows of 4096, groups of 64, three vectors 52.5 us (286 MB,
+// 5.4 TB/s, 0.80 of the copy bandwidth; 61 % of the issue slots, 62 % of the L1
+// data path); 24576 rows (SwiGLU), one vector 14.8 us (3.5 TB/s: 4 us of it are
+// launch, staging and the last tiles; 49 % of the issue slots); 4096 x 4096, one
+// vector 5.0 us; 4096 x 12288, groups of 32, 13 vectors 14.6 us (43 % of the
+// issue slots).
 struct W4Args {
   const uint8_t* w;
   const uint16_t* scale;
@@ -338,13 +333,23 @@ constexpr int kW4Chunks = 4;  // chunks of an item
 constexpr int kW4Pitch = 20;  // floats between the columns of a warp's part: conflict-free fragment stores
 
 // d = a b + c.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, "
-      "%13};"
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+      "%12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// The codes in the lowest four bits of w's halves, and those four bits further
+// up, as pairs of bf16 q 2^-6.
+constexpr uint32_t kBf2m3 = 0xBE00BE00u;  // -2^-3, twice
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, kBf2m3); }  // 2^127
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, kBf2m3); }  // 2^123
 // The scales of a row's item: lane c of the row's four holds the 128 / G of
 // chunk c, so that one load fetches an item's (a load of 8 rows costs the L1
 // data path 8 cycles, whatever it fetches of each; with each lane loading
@@ -374,12 +379,10 @@ struct W4Scales {
 };
 
 // Shared memory: the warps' parts of two tiles [2][8][8 NT vectors][20],
-// (cluster) finished parts [slots][teams][8 NT][16], then per group and vector
-// -8 2^-24 sum x 2^-e, per item and vector 2^e, then the vectors, as f16 in their order, 64 bytes
-// between them so that two neighbours lie in different halves of the banks.
-// Columns that no vector has take the last vector and whatever sums lie in
-// their place: a column's sums depend on that column alone, and theirs are
-// read by nobody.
+// (cluster) finished parts [slots][teams][8 NT][16], then the vectors in their
+// order, 64 bytes between them so that two neighbours lie in different halves of
+// the banks.  Columns that no vector has take the last vector: a column's sums
+// depend on that column alone, and theirs are read by nobody.
 template <int NT>
 struct W4Smem {
   static constexpr int part = NT * 8 * kW4Pitch;  // floats of a warp's part
@@ -387,12 +390,6 @@ struct W4Smem {
   static constexpr int res = NT * 128 * 4;  // of a slot
 };
 __host__ __device__ constexpr int w4_pitch(int segc) { return segc * 256 + 64; }
-__host__ __device__ constexpr int w4_sum_bytes(int segc, int group, int nt) {
-  return (segc * (128 / group) + segc / kW4Chunks) * nt * 32;
-}
-__host__ __device__ constexpr int w4_x_bytes(int B, int segc, int group, int nt) {
-  return w4_sum_bytes(segc, group, nt) + B * w4_pitch(segc);
-}
 
 __device__ __forceinline__ void w4_store(const W4Args& a, int n, int col, float v) {
   if (a.f32_out)
@@ -401,79 +398,26 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int n, int col, float 
     static_cast<uint16_t*>(a.y)[(long long)col * a.n_out + n] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
 }
 
-// The block's part of the vectors to f16 times 2^-e, each group's share of the
-// correction, -8 2^-24 sum x 2^-e, and each item's 2^e to `up`.  Elements
-// beyond K are zeros.  A warp takes the 512 elements of an item of one vector
-// at a time, with U items' loads in flight.
-template <int G, int NT>
-__device__ __forceinline__ void w4_stage(const W4Args& a, int c0, float* fx, float* up, uint8_t* xs) {
-  constexpr int GL = G / 8;  // lanes of a group
-  constexpr int U = 4;
-  const int pitch = w4_pitch(a.segc), per = a.segc / kW4Chunks, n = a.B * per;  // items of a vector, of all
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  struct Piece {  // item j of vector b
-    int b, j;
-    __device__ __forceinline__ void next(int per) {
-      j += kW4Warps;
-      while (j >= per) j -= per, ++b;
-    }
-  };
-  Piece p{0, warp - kW4Warps};
-  p.next(per);
-  uint4 u[U][2];
-  Piece q = p;  // the next one to load
-  auto fetch = [&](int t) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = c0 * 128 + q.j * 512 + 256 * h + 8 * lane;
-      u[t][h] = make_uint4(0, 0, 0, 0);
-      if (q.b < a.B && k < a.K) u[t][h] = __ldg(reinterpret_cast<const uint4*>(a.x + (long long)q.b * a.K + k));
-    }
-    q.next(per);
-  };
-#pragma unroll
-  for (int t = 0; t < U; ++t) fetch(t);
-#pragma unroll 1
-  for (int i0 = warp; i0 < n; i0 += U * kW4Warps) {
-#pragma unroll
-    for (int t = 0; t < U; ++t) {
-      if (i0 + t * kW4Warps >= n) break;  // the same for the whole warp
-      unsigned m = 0;  // |x| as bits, two at once
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(u[t][h].x & 0x7FFF7FFFu, u[t][h].y & 0x7FFF7FFFu),
-                                 __vmaxu2(u[t][h].z & 0x7FFF7FFFu, u[t][h].w & 0x7FFF7FFFu)));
-      m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
-      // an item with an infinity or a NaN yields NaNs whatever its factor
-      const int e = min(max((int)(m >> 7) - 127 - 14, -112), 112);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      if (lane == 0) up[p.j * (8 * NT) + p.b] = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w[4] = {u[t][h].x, u[t][h].y, u[t][h].z, u[t][h].w};
-        uint32_t h4[4];
-        float part[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float f = (k & 1) ? down * 0.0625f : down;  // elements 2, 3 and 6, 7 meet 16 n
-          const float lo = bf16_lo(w[k]) * f, hi = bf16_hi(w[k]) * f;
-          part[k & 1] += lo + hi;
-          const __half2 h2 = __floats2half2_rn(lo, hi);
-          h4[k] = *reinterpret_cast<const uint32_t*>(&h2);
-        }
-        *reinterpret_cast<uint4*>(xs + p.b * pitch + p.j * 1024 + h * 512 + lane * 16) =
-            make_uint4(h4[0], h4[1], h4[2], h4[3]);
-        float sum = fmaf(16.0f, part[1], part[0]);
-#pragma unroll
-        for (int o = 1; o < GL; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % GL == 0)
-          fx[((2 * p.j + h) * (256 / G) + lane / GL) * (8 * NT) + p.b] = sum * (-8.0f / 16777216.0f);
-      }
-      p.next(per);
-      fetch(t);
-    }
+// Copies the block's part of the vectors, 16 bytes at a time, zeros beyond K
+// (a multiple of 32: no piece is cut).  Asynchronous, every piece in flight at
+// once; the caller waits for its own with stage_wait and for the others' with a
+// barrier.
+__device__ __forceinline__ void w4_stage(const W4Args& a, int c0, uint8_t* xs) {
+  const int per = a.segc * 16, pitch = w4_pitch(a.segc);  // pieces of a vector
+  const int db = kW4Warps * 32 / per, dj = kW4Warps * 32 - db * per;
+  int b = threadIdx.x / per, j = threadIdx.x - b * per;
+  const uint32_t dst = smem_u32(xs);
+  while (b < a.B) {
+    const int k = c0 * 128 + 8 * j;
+    const uint16_t* src = a.x + (long long)b * a.K + min(k, a.K - 8);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + b * pitch + 16 * j), "l"(src),
+                 "r"(k < a.K ? 16 : 0)
+                 : "memory");
+    b += db, j += dj;
+    if (j >= per) j -= per, ++b;
   }
 }
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Codes are read once: not kept in L1.  An item's 256 bytes of a row come to L2
 // with the first of its four loads (logits 54.1 to 51.7 us).
@@ -497,9 +441,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) gemv_w4_kernel(const W4Args 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int team = warp >> a.team_log, wt = warp & (a.team - 1), teams = kW4Warps >> a.team_log;
-  float* fx = res + (CL ? a.slots * teams * (SM::res / 4) : 0);
-  float* up = fx + a.segc * (128 / G) * 8 * NT;
-  uint8_t* xs = reinterpret_cast<uint8_t*>(fx) + w4_sum_bytes(a.segc, G, NT);
+  uint8_t* xs = reinterpret_cast<uint8_t*>(res + (CL ? a.slots * teams * (SM::res / 4) : 0));
   volatile int* abort_flag = &sh_abort;
   const uint32_t part_full0 = smem_u32(bars + 4 * team), part_free0 = part_full0 + 16;  // [2] per buffer of parts
   const int csize = CL ? 1 << a.cluster_log : 1, rank = CL ? (int)cluster_ctarank() : 0;
@@ -556,6 +498,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) gemv_w4_kernel(const W4Args 
 #pragma unroll
     for (int ci = 0; ci < CW; ++ci) load_chunk(0, ci);
   }
+  w4_stage(a, c0, xs);
 
   if (lane == 0) {
     if (wt == 0)
@@ -563,7 +506,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) gemv_w4_kernel(const W4Args 
     if (warp == 0) sh_abort = 0;
     fence_barrier_init();
   }
-  w4_stage<G, NT>(a, c0, fx, up, xs);
+  stage_wait();
   __syncthreads();
 
   float y[NT][4];  // rows g and g + 8, vectors 8 nt + 2 c and + 1
@@ -608,7 +551,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) gemv_w4_kernel(const W4Args 
     for (int i = 0; i < 4 * NT; ++i) {
       if (2 * i >= a.B) break;
       const int col = 2 * i + (lane >> 4);
-      v[i] *= 16777216.0f;  // out of the units of 2^-24
+      v[i] *= 64.0f;  // out of the units of 2^-6
       if (CL) {
         if (col < a.B) res[(((k % a.slots) << (kW4WarpsLog - a.team_log)) + team) * NT * 128 + col * 16 + r] = v[i];
       } else {
@@ -636,62 +579,46 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) gemv_w4_kernel(const W4Args 
           for (int hh = 0; hh < 2; ++hh) wp[hh] += step * 64, sp[hh] += step * (128 / G), left[hh] -= stride * rpt;
         }
         if (more) load_scales(ni);
-        // Chunks beyond K meet zeros: x and its sums are zero there, up to whole
-        // items, and the registers hold some codes and some finite scales.
-        const float* fj = fx + j0 * (128 / G) * (8 * NT) + 2 * c;
+        // Chunks beyond K meet zeros: x is zero there, up to whole items, and the
+        // registers hold some codes and some finite scales.
         const uint8_t* xj[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) xj[nt] = xrow[nt] + j0 * 256;
-        float z[NT][4];  // the item's sums
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) z[nt][0] = z[nt][1] = z[nt][2] = z[nt][3] = 0.f;
 #pragma unroll
         for (int ci = 0; ci < CW; ++ci) {
           const W4Scales<G> sg = sv[0].of(ci), sh = sv[1].of(ci);
           float acc[NT][4];
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
-            uint4 xb[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) xb[nt] = *reinterpret_cast<const uint4*>(xj[nt] + ci * 256 + i4 * 64);
             if (32 * i4 % G == 0) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {  // the correction of columns 2 c and 2 c + 1
-                const float2 f =
-                    *reinterpret_cast<const float2*>(fj + (ci * (128 / G) + 32 * i4 / G) * (8 * NT) + nt * 8);
-                acc[nt][0] = acc[nt][2] = f.x, acc[nt][1] = acc[nt][3] = f.y;
-              }
+              for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
             }
             const uint4 &lo = wv[ci][0], &hi = wv[ci][1];
             const uint32_t wg = i4 == 0 ? lo.x : i4 == 1 ? lo.y : i4 == 2 ? lo.z : lo.w;
             const uint32_t wh = i4 == 0 ? hi.x : i4 == 1 ? hi.y : i4 == 2 ? hi.z : hi.w;
             const uint32_t vg = wg >> 8, vh = wh >> 8;
+            const uint32_t q0 = codes_lo(wg), q1 = codes_lo(wh), q2 = codes_hi(wg), q3 = codes_hi(wh);
+            const uint32_t q4 = codes_lo(vg), q5 = codes_lo(vh), q6 = codes_hi(vg), q7 = codes_hi(vh);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              const uint4 xb = *reinterpret_cast<const uint4*>(xj[nt] + ci * 256 + i4 * 64);
               float(&q)[4] = acc[nt];
-              mma_f16(q, wg & 0x000F000Fu, wh & 0x000F000Fu, wg & 0x00F000F0u, wh & 0x00F000F0u, xb[nt].x, xb[nt].y,
-                      q[0], q[1], q[2], q[3]);
-              mma_f16(q, vg & 0x000F000Fu, vh & 0x000F000Fu, vg & 0x00F000F0u, vh & 0x00F000F0u, xb[nt].z, xb[nt].w,
-                      q[0], q[1], q[2], q[3]);
+              mma_bf16(q, q0, q1, q2, q3, xb.x, xb.y, q[0], q[1], q[2], q[3]);
+              mma_bf16(q, q4, q5, q6, q7, xb.z, xb.w, q[0], q[1], q[2], q[3]);
             }
             if (32 * (i4 + 1) % G == 0) {
               const float s0 = sg.get(32 * i4 / G), s1 = sh.get(32 * i4 / G);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                z[nt][0] = fmaf(s0, acc[nt][0], z[nt][0]);
-                z[nt][1] = fmaf(s0, acc[nt][1], z[nt][1]);
-                z[nt][2] = fmaf(s1, acc[nt][2], z[nt][2]);
-                z[nt][3] = fmaf(s1, acc[nt][3], z[nt][3]);
+                y[nt][0] = fmaf(s0, acc[nt][0], y[nt][0]);
+                y[nt][1] = fmaf(s0, acc[nt][1], y[nt][1]);
+                y[nt][2] = fmaf(s1, acc[nt][2], y[nt][2]);
+                y[nt][3] = fmaf(s1, acc[nt][3], y[nt][3]);
               }
             }
           }
           if (more) load_chunk(ni, ci);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {  // 2^e of columns 2 c and 2 c + 1
-          const float2 f = *reinterpret_cast<const float2*>(up + j0 / CW * (8 * NT) + nt * 8 + 2 * c);
-          y[nt][0] = fmaf(z[nt][0], f.x, y[nt][0]), y[nt][1] = fmaf(z[nt][1], f.y, y[nt][1]);
-          y[nt][2] = fmaf(z[nt][2], f.x, y[nt][2]), y[nt][3] = fmaf(z[nt][3], f.y, y[nt][3]);
         }
       }
       // the warp's part of the tile goes to one of two buffers
@@ -768,7 +695,7 @@ int w4_segment(int nch, int csize) { return ((nch + csize - 1) / csize + kW4Chun
 
 template <int G, int NT>
 int w4_least(int B, int segc, bool cl) {
-  return W4Smem<NT>::red + (cl ? W4Smem<NT>::res : 0) + w4_x_bytes(B, segc, G, NT);
+  return W4Smem<NT>::red + (cl ? W4Smem<NT>::res : 0) + B * w4_pitch(segc);
 }
 
 // Tiles of a team between two exchanges of a cluster, with `left` bytes beside
@@ -791,9 +718,10 @@ struct W4Plan {
 // In cycles of an SM, as measured: 17 for a chunk of a vector (every SM reads
 // the same lines of L2, at 15 bytes a cycle), 3000 for an item of each of 16
 // warps (4000 with more than 8 vectors), 10000 for an exchange with the wait
-// for the slowest block.  13 vectors, 4096 rows: K = 12288 took 18.8 us in
-// clusters of 4, 22.8 of 2, 28.9 of 8; K = 4096 took 9.5 us without, 9.8 in
-// clusters of 4, 10.2 of 2.
+// for the slowest block.  13 vectors, 4096 rows: K = 12288 took 14.9 us in
+// clusters of 4, 17.4 of 2, 24.9 of 8; K = 4096 took 8.4 us without, 8.4 in
+// clusters of 4, 8.6 of 2; the cut chosen was within 3 % of the fastest one for
+// ten shapes of 1 to 16 vectors.
 template <int G, int NT>
 W4Plan w4_plan(const W4Args& a, int csize, int most, double& cost) {
   W4Plan p = {csize, w4_segment(a.nch, csize), 0, 0};

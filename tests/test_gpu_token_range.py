@@ -1,11 +1,13 @@
 """The token-step operators where the range of the numbers or of the bounds is wide: scores far from zero, one token
 that outweighs many small ones, elements that outweigh the rest of a vector, bounds far above the lengths."""
+import math
+
 import pytest
 import torch
 
 from diffusion_transformer_image_mmdit_gb300 import api
 from tests import token_oracle as T
-from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn,
+from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn, w4_case,
                                       within)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +99,91 @@ def test_kv_attention_query_channel_that_meets_zero_keys(d):
     o, mag = p @ vv, (qq.abs() @ kk.abs().t() * d ** -0.5).amax(1, keepdim=True)
     tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2.0 ** -18 + mag * 2.0 ** -19) * 1.01 * (p @ vv.abs()) + 256 * 2.0 ** -39 * vv.abs().amax()
     within(out.view(2, d), o, tol, "outlier channel")
+
+
+# ------------------------------------------------------------------ 4-bit products
+# A product of an element and a code is exact; a term passes at most 16 sums of an instruction, 8 of a group, K / 1024 + 1
+# scaled groups and the parts of 16 warps and 8 blocks, each off by 2^-23 of what is summed (matrix sums cut off).
+def exact_tol(x, w, bias, K):
+    return 2.0 ** -23 * (16 + 8 + K / 256 + 16) * (x.abs() @ w.abs().t() + bias.abs())
+
+
+def zero_columns(g, N, K, group, cols):
+    w = 0.02 * randn(g, N, K)
+    w[:, cols] = 0
+    lin = api.quantize_linear_w4(api.LinearDev(w.to(BF16).cuda(), (0.1 * randn(g, N)).cuda()), group)
+    w64 = T.w4_weights(lin.w.cpu(), lin.scale.cpu(), group, K)
+    assert not w64[:, cols].any()
+    return lin, w64
+
+
+def product(lin, x):
+    y = torch.empty(x.shape[0], lin.N, device="cuda")
+    api.mmdit_gemv_w4(lin, x.cuda(), y, api.MMDIT_EPI_F32)
+    return y.cpu()
+
+
+@pytest.mark.parametrize("B", [1, 13])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("exp", [10, 20, 40, 120])
+def test_gemv_w4_element_that_meets_zero_codes(B, group, exp):
+    """Elements far above the rest of their vector whose codes are 0 take nothing from the others' products."""
+    g = gen(exp + group)
+    K, N, cols = 4096, 200, [7, 1000, 4095]
+    lin, w = zero_columns(g, N, K, group, cols)
+    x = randn(g, B, K).to(BF16)
+    x[:, cols] = torch.tensor([2.0, -2.0, 1.5], dtype=BF16) * 2.0 ** exp
+    b = lin.b.cpu().to(F64)
+    xx = x.to(F64)
+    rest = xx.clone()
+    rest[:, cols] = 0
+    within(product(lin, x), xx @ w.t() + b, exact_tol(rest, w, b, K), "others")
+
+
+def test_gemv_w4_elements_of_all_sizes():
+    """Vectors whose elements span the range of the type, items of zeros, and the largest and smallest alone."""
+    g = gen(70)
+    K, N = 2048, 150
+    lin, w = w4_case(g, N, K, 64)
+    x = (randn(g, 12, K) * torch.exp2(torch.randint(-90, 91, (12, K), generator=g))).to(BF16)
+    x[1, 512:] = 0
+    x[2, :1024] = 0
+    x[3] = (randn(g, K) * 2.0 ** -100).to(BF16)
+    x[4], x[5] = 0, 0
+    x[4, 600] = 2.0 ** 127
+    x[5, 900] = 2.0 ** -100
+    x[6] = (randn(g, K) * torch.exp2(torch.randint(0, 40, (K,), generator=g))).to(BF16)
+    lin = api.LinearW4Dev(lin.w, lin.scale, 64, K)
+    xx = x.to(F64)
+    within(product(lin, x), xx @ w.t(), exact_tol(xx, w, torch.zeros(N, dtype=F64), K) * (1 + 1e-9), "sizes")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_gemv_w4_of_unit_vectors_is_the_weights(group):
+    """A vector of one element gives a column of W, bit for bit: every code, in every place of a word, in every chunk."""
+    g = gen(group)
+    K, N = 3 * 128 if group == 128 else 3 * 128 + group, 64
+    q = torch.randint(0, 256, (N, api.w4_row_bytes(K)), generator=g).to(torch.uint8)
+    s = torch.exp2(randn(g, N, (K + 127) // 128 * (128 // group))).to(BF16)
+    lin = api.LinearW4Dev(q.cuda(), s.cuda(), group, K)
+    w = T.w4_weights(q, s, group, K)
+    for k0 in range(0, K, 16):
+        x = torch.zeros(16, K, dtype=BF16)
+        x[range(16), range(k0, k0 + 16)] = 1
+        assert torch.equal(product(lin, x).to(F64), w[:, k0:k0 + 16].t())
+
+
+def test_gemv_w4_infinities():
+    """An infinity gives what the definition does: an infinity where its code is not 0, a NaN where it is."""
+    g = gen(71)
+    K, N = 1024, 300
+    lin, w = w4_case(g, N, K, 32)
+    x = randn(g, 5, K).to(BF16)
+    x[0, 3], x[1, 700], x[2, 5], x[2, 900], x[3, 10] = math.inf, -math.inf, math.inf, -math.inf, math.nan
+    y, ref = product(lin, x).to(F64), torch.empty(5, N, dtype=F64)
+    for i in range(5):
+        ref[i] = (x[i].to(F64) * w).sum(1) + lin.b.cpu().to(F64)
+    assert bool((w[:, 3] == 0).any()) and bool(torch.isinf(ref[0]).any()) and bool(torch.isnan(ref[0]).any())
+    assert torch.equal(torch.isnan(y), torch.isnan(ref))
+    inf = torch.isinf(ref)
+    assert torch.equal(torch.isinf(y), inf) and torch.equal(y[inf], ref[inf])
