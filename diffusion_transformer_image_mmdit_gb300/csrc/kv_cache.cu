@@ -55,9 +55,9 @@ struct KvPtrs {
 // arrays have them; and whether they lie within the cache and the rows.
 __device__ __forceinline__ int3 kv_seq_raw(const KvPtrs& p, int b) {
   int3 r;  // volatile: asked for where the code says, which is ahead of use
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r.x) : "l"(p.start + b));
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r.y) : "l"(p.start + b + 1));
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r.z) : "l"(p.len + b));
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.x) : "l"(p.start + b));
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.y) : "l"(p.start + b + 1));
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.z) : "l"(p.len + b));
   return r;
 }
 __device__ __forceinline__ bool kv_seq_ok(const KvDims& d, int3 r) {
@@ -87,8 +87,8 @@ struct AppendArgs {
 // d / 2 behind them, so that a lane holds both of each pair.
 template <bool HALVES>
 __device__ __forceinline__ uint4 load_head(const uint16_t* first, int second) {
-  if (!HALVES) return __ldg(reinterpret_cast<const uint4*>(first));
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(first)), b = __ldg(reinterpret_cast<const uint2*>(first + second));
+  if (!HALVES) return *reinterpret_cast<const uint4*>(first);
+  const uint2 a = *reinterpret_cast<const uint2*>(first), b = *reinterpret_cast<const uint2*>(first + second);
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 
@@ -96,8 +96,8 @@ __device__ __forceinline__ uint4 load_head(const uint16_t* first, int second) {
 struct Turn {
   float c[4], s[4];
   __device__ __forceinline__ void load(int v, int half, long long pos, const float* cs, const float* sn) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(cs + pos * half + 4 * v));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(sn + pos * half + 4 * v));
+    const float4 a = *reinterpret_cast<const float4*>(cs + pos * half + 4 * v);
+    const float4 b = *reinterpret_cast<const float4*>(sn + pos * half + 4 * v);
     c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
     s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
   }
@@ -126,8 +126,8 @@ __device__ __forceinline__ void head_norm8(float* x, int v, const float* g, floa
 #pragma unroll
   for (int o = VH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   const float r = rsqrtf(ss * (1.0f / (VH * 8)) + eps);
-  const float4 a = __ldg(reinterpret_cast<const float4*>(g + (HALVES ? 4 : 8) * v));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(g + (HALVES ? VH * 4 + 4 * v : 8 * v + 4)));
+  const float4 a = *reinterpret_cast<const float4*>(g + (HALVES ? 4 : 8) * v);
+  const float4 b = *reinterpret_cast<const float4*>(g + (HALVES ? VH * 4 + 4 * v : 8 * v + 4));
   const float gg[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = x[i] * r * gg[i];
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
       if (slot >= lo && slot < hi && n < nh) u[n][p] = load_head<HALVES>(r + n * HD, second);
     }
   }
-  const int id = __ldg(a.p.table + (long long)b * d.table_ld + blk);
+  const int id = a.p.table[(long long)b * d.table_ld + blk];
   if (id < 0 || id >= d.n_blocks) {
     if (tid == 0 && h == 0) atomicOr(a.p.status, kStatusBadIndex);
     return;
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
     int t_first = -1;
     {
       const int j = j0 + warp + kKvWarps * lane;
-      if (j < j_end) t_first = j0 == 0 && ahead_b == b ? ahead : __ldg(a.p.table + (long long)b * d.table_ld + j);
+      if (j < j_end) t_first = j0 == 0 && ahead_b == b ? ahead : a.p.table[(long long)b * d.table_ld + j];
     }
 
     // the lane's part of the queries (channels 16 c .. 16 c + 15 of each 64 of
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
 #pragma unroll
       for (int i = 0; i < HD / 32; ++i) {
         qr[nt][i] = make_uint4(0, 0, 0, 0);
-        if (nt * 8 + g < rows) qr[nt][i] = __ldg(reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 8 * (i & 1)));
+        if (nt * 8 + g < rows) qr[nt][i] = *reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 8 * (i & 1));
       }
     }
 
@@ -709,11 +709,11 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
       const int j = j0 + warp + kKvWarps * (i + lane);
       id_n = 0, ks_n = 0.f, vs_n = 0.f;
       if (j < j_end) {
-        const int t = i == 0 ? t_first : __ldg(a.p.table + (long long)b * d.table_ld + j);
+        const int t = i == 0 ? t_first : a.p.table[(long long)b * d.table_ld + j];
         if (t >= 0 && t < d.n_blocks) {
           id_n = t;
-          ks_n = __ldg(a.p.ks + (long long)t * d.Hkv + h);
-          vs_n = __ldg(a.p.vs + (long long)t * d.Hkv + h);
+          ks_n = a.p.ks[(long long)t * d.Hkv + h];
+          vs_n = a.p.vs[(long long)t * d.Hkv + h];
         } else {
           id_n = -1, ks_n = 1.f;  // left out: its keys are masked
           atomicOr(a.p.status, kStatusBadIndex);
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
       const int n = same ? sq.len : b + 1 < d.B && kv_seq_ok(d, next) ? next.z : 0;
       ahead = -1;
       if (x + took < x1 && j < (n + kBlk - 1) / kBlk)
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(ahead) : "l"(a.p.table + (long long)ahead_b * d.table_ld + j));
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(ahead) : "l"(a.p.table + (long long)ahead_b * d.table_ld + j));
     }
 
     // Q^T operand

@@ -18,6 +18,10 @@ __device__ __forceinline__ uint16_t f8x2_e4m3(float lo, float hi) {
 // is visible then.  Only behind that does it let the next kernel start
 // (`grid_release`), so that whatever comes on early finds all but its direct
 // predecessor ended.
+// What such a kernel reads may thus be written while it is resident: it uses no
+// non-coherent loads (__ldg, ld.global.nc), which are for data that nobody
+// writes during the whole kernel and which the compiler may raise above the
+// wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
