@@ -301,12 +301,13 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const void* __restrict
 // cluster of blocks splits K and adds the parts up through distributed shared
 // memory.
 //
-// Measured: 131071 rows of 4096, groups of 64, three vectors 52.5 us (286 MB,
-// 5.4 TB/s, 0.80 of the copy bandwidth; 61 % of the issue slots, 62 % of the L1
-// data path); 24576 rows (SwiGLU), one vector 14.8 us (3.5 TB/s: 4 us of it are
+// Measured: 131071 rows of 4096, groups of 64, three vectors 52.0 us (286 MB,
+// 5.5 TB/s, 0.81 of the copy bandwidth; 61 % of the issue slots, 62 % of the L1
+// data path); 24576 rows (SwiGLU), one vector 14.7 us (3.5 TB/s: 4 us of it are
 // launch, staging and the last tiles; 49 % of the issue slots); 4096 x 4096, one
-// vector 5.0 us; 4096 x 12288, groups of 32, 13 vectors 14.6 us (43 % of the
-// issue slots).
+// vector 5.1 us; 4096 x 12288, groups of 32, 13 vectors 14.2 us (43 % of the
+// issue slots).  Two accumulators per group, for the even and odd words, are no
+// faster: 53.2, 15.2, 5.9 and 14.9 us where one had 52.3, 15.1, 5.8 and 14.5.
 struct W4Args {
   const uint8_t* w;
   const uint16_t* scale;
@@ -358,8 +359,7 @@ template <int G>
 struct W4Scales {
   static constexpr int W = G == 32 ? 2 : 1;
   uint32_t v[W];
-  // volatile: asked for where the code says (as plain loads they came on later,
-  // 4096 x 4096 5.9 us for 5.1)
+  // volatile: asked for where the code says
   __device__ __forceinline__ void load(const uint16_t* p) {
     if (G == 32) {
       asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[W - 1]) : "l"(p));
@@ -403,8 +403,8 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int n, int col, float 
 
 // Copies the block's part of the vectors, 16 bytes at a time, zeros beyond K
 // (a multiple of 32: no piece is cut).  Asynchronous, every piece in flight at
-// once; the caller waits for its own with stage_wait and for the others' with a
-// barrier.
+// once, and through L1 (4096 x 4096, one vector 5.1 us; past it 5.8); the caller
+// waits for its own with stage_wait and for the others' with a barrier.
 __device__ __forceinline__ void w4_stage(const W4Args& a, int c0, uint8_t* xs) {
   const int per = a.segc * 16, pitch = w4_pitch(a.segc);  // pieces of a vector
   const int db = kW4Warps * 32 / per, dj = kW4Warps * 32 - db * per;
@@ -413,7 +413,7 @@ __device__ __forceinline__ void w4_stage(const W4Args& a, int c0, uint8_t* xs) {
   while (b < a.B) {
     const int k = c0 * 128 + 8 * j;
     const uint16_t* src = a.x + (long long)b * a.K + min(k, a.K - 8);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + b * pitch + 16 * j), "l"(src),
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + b * pitch + 16 * j), "l"(src),
                  "r"(k < a.K ? 16 : 0)
                  : "memory");
     b += db, j += dj;
