@@ -1055,17 +1055,22 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
   }
 }
 
-// Adds up the parts of the units that were cut: one block per unit and row, its
+// Adds up the parts of the units that were cut, one block per unit and row, its
 // W warps taking every W-th part (a long sequence alone is cut into as many
-// parts as its kv head has thread blocks), then merged in a fixed order.  Few
-// registers (32 per thread; 51 with 16 warps): blocks come on an SM beside one
-// of the attention's, and find their unit while others still read.
+// parts as its kv head has thread blocks), then merged in a fixed order.  The
+// grid's x dimension goes over the units or, where fewer (as with many tokens,
+// or bounds above the lengths: units are numbered by the shape's bounds), over
+// the boundaries between the attention's blocks: a unit that is cut is merged by
+// the first boundary inside it.  Few registers (32 per thread; 51 with 16
+// warps): blocks come on an SM beside one of the attention's, and find their
+// unit while others still read.
 template <int HD, int NT, int W>
-__global__ void __launch_bounds__(W * 32) kv_combine_kernel(const KvAttnArgs a, int grid, int rt_max) {
+__global__ void __launch_bounds__(W * 32) kv_combine_kernel(const KvAttnArgs a, int grid, int rt_max, int by_unit) {
   constexpr int R = 8 * NT;
   constexpr int CL = HD / 32;  // channels of a lane
   __shared__ long long sh_scan[W];
   __shared__ long long sh_base;
+  __shared__ int sh_b;
   __shared__ float sh_o[W][HD];
   __shared__ float2 sh_ml[W];
   // This grid starts while the attention's last blocks run: everything up to
@@ -1074,30 +1079,54 @@ __global__ void __launch_bounds__(W * 32) kv_combine_kernel(const KvAttnArgs a, 
   // those with nothing to do: what follows in the stream counts on both.
   const KvDims& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = blockIdx.y;
-  const int r = blockIdx.x % rt_max, h = (blockIdx.x / rt_max) % d.Hkv, b = blockIdx.x / rt_max / d.Hkv;
-  const KvSeq sq = kv_units<R>(a, kv_seq_raw(a.p, b));
-  if (r >= sq.rt || row >= sq.T * d.G - r * R) {  // the same for the whole block
-    grid_wait();
-    grid_release();
-    return;
+  auto nothing = [] { grid_wait(), grid_release(); };
+  int b = by_unit ? blockIdx.x / rt_max / d.Hkv : 0;
+  KvSeq sq;
+  if (by_unit) {
+    sq = kv_units<R>(a, kv_seq_raw(a.p, b));
+    const int r = blockIdx.x % rt_max;
+    if (r >= sq.rt || row >= sq.T * d.G - r * R) return nothing();  // the same for the whole block
   }
-  long long total = 0;
+  long long total = 0, w = 0, before = 0;
   for (int b0 = 0; b0 < d.B; b0 += W * 32) {
-    long long before;
-    const long long w = b0 + tid < d.B ? kv_units<R>(a, kv_seq_raw(a.p, b0 + tid)).w : 0;
+    w = b0 + tid < d.B ? kv_units<R>(a, kv_seq_raw(a.p, b0 + tid)).w : 0;
     const long long all = block_scan(w, before, sh_scan);
-    if (b0 + tid == b) sh_base = total + before;
+    if (by_unit && b0 + tid == b) sh_base = total + before;
     total += all;
   }
+  const int ctas = kv_ctas(total, grid, 1), cut = blockIdx.x + 1;  // boundary: block `cut` begins at x
+  long long x = 0;
+  if (!by_unit) {
+    if (cut >= ctas || total == 0) return nothing();
+    x = div_pos(total * cut, ctas);
+    long long at = 0;
+    for (int b0 = 0; b0 < d.B; b0 += W * 32) {  // the sequence that x lies in
+      long long all = total;
+      if (d.B > W * 32) {  // else the scan above was the only one
+        w = b0 + tid < d.B ? kv_units<R>(a, kv_seq_raw(a.p, b0 + tid)).w : 0;
+        all = block_scan(w, before, sh_scan);
+      }
+      if (w > 0 && at + before <= x && x < at + before + w) sh_b = b0 + tid, sh_base = at + before;
+      at += all;
+    }
+  }
   __syncthreads();
-  const int ctas = kv_ctas(total, grid, 1);
-  const long long u0 = sh_base + ((long long)h * sq.rt + r) * sq.nb, u1 = u0 + sq.nb - 1;
+  const long long base = sh_base;
+  int h = (blockIdx.x / rt_max) % d.Hkv, r = blockIdx.x % rt_max;
+  if (!by_unit) {
+    b = sh_b;
+    sq = kv_units<R>(a, kv_seq_raw(a.p, b));
+    const long long unit = div_pos(x - base, sq.nb);
+    h = (int)div_pos(unit, sq.rt), r = (int)(unit - (long long)h * sq.rt);
+    if (row >= sq.T * d.G - r * R) return nothing();
+  }
+  const long long u0 = base + ((long long)h * sq.rt + r) * sq.nb, u1 = u0 + sq.nb - 1;
   // the block with the largest number c such that total c / ctas <= u, for the
   // unit's first and last block
   const int c0 = (int)(((u0 + kKvUnitCost + 1) * ctas + total - 1) / total) - 1, c1 = (int)(((u1 + 1) * ctas + total - 1) / total) - 1;
+  if (c0 == c1 || (!by_unit && c0 != cut - 1)) return nothing();  // not cut, or not here first
   grid_wait();
   grid_release();
-  if (c0 == c1) return;  // not cut
   const float* stat = a.part + (long long)grid * 2 * R * HD;
   const bool first = total * c0 / ctas >= u0;  // block c0 begins with this unit
   float m = -INFINITY, l = 0.f, o[CL];
@@ -1173,13 +1202,15 @@ cudaError_t launch_kv_attention(KvAttnArgs a, cudaStream_t st) {
   launch_end(st);
   if (e != cudaSuccess || !a.split) return e;
   launch_begin(KID_KV_COMBINE, st);
-  const dim3 rows((unsigned)units, (unsigned)std::min<long long>(R, (long long)a.d.max_new * a.d.G));
+  const int by_unit = units < grid;
+  const dim3 rows((unsigned)(by_unit ? units : std::max(1, grid - 1)),
+                  (unsigned)std::min<long long>(R, (long long)a.d.max_new * a.d.G));
   // Few rows to merge have many parts each.  One sequence of 131069 takes 51.4
   // us with 16 warps a row, 53 with 8, 54.3 with 4, 57.4 with 2; 48 sequences
   // 81.8, 73.1, 70.0 and 70.1; 8 sequences 28.5 with 16, 28.8 with 4.
   const bool few = (long long)rows.x * rows.y <= 2 * num_sms();
   e = launch_after(few ? kv_combine_kernel<HD, NT, 16> : kv_combine_kernel<HD, NT, 4>, rows, dim3(few ? 512 : 128), 0, 1, st,
-                   a, grid, (int)rt);
+                   a, grid, (int)rt, by_unit);
   launch_end(st);
   return e;
 }

@@ -101,6 +101,43 @@ def test_kv_attention_query_channel_that_meets_zero_keys(d):
     within(out.view(2, d), o, tol, "outlier channel")
 
 
+def device_us(f, n=5):
+    f()
+    best = math.inf
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+def test_kv_attention_bounds_far_above_the_lengths():
+    """One new token in each of 48 sequences under a bound of 8192 new tokens: the answer of the tight bound, and about its
+    time (the merge's grid does not grow with the bound; a factor of 4 and 300 us are left for the launches)."""
+    g = gen(65)
+    sq = Seqs(g, [int(n) for n in torch.randint(600, 4000, (48,), generator=g)], [1] * 48)
+    tokens = random_cache(g, sq.n_blocks, 8, 64)
+    k, v, ks, vs = tokens[0] & 0x77, tokens[1] & 0x77, *tokens[2:]
+    cache = device_cache(k, v, ks, vs, sq)
+    q = randn(g, 48, 32 * 64).to(BF16).cuda()
+    took, outs = [], []
+    for kw in (dict(), dict(max_new=3, max_len=5000), dict(max_new=8192, max_len=8192)):
+        # a table wide enough for the largest bound
+        kw["table_ld"] = 128
+        wide = api.KVCacheDev(cache.k, cache.v, cache.k_scale, cache.v_scale,
+                              torch.nn.functional.pad(cache.table, (0, 128 - cache.table.shape[1])), cache.len, cache.start)
+        shape = sq.shape(32, 8, 64, **kw)
+        ws, out = api.alloc_workspace(api.kv_workspace_size(shape)), torch.empty_like(q)
+        took.append(device_us(lambda: api.mmdit_kv_attention(shape, wide, q, out, ws)))
+        outs.append(out.float())
+    for o in outs[1:]:
+        assert float((o - outs[0]).abs().max()) <= 2.0 ** -6 * float(outs[0].abs().max())
+    assert max(took[1:]) <= 4 * took[0] + 300, took
+
+
 # ------------------------------------------------------------------ 4-bit products
 # A product of an element and a code is exact; a term passes at most 16 sums of an instruction, 8 of a group, K / 1024 + 1
 # scaled groups and the parts of 16 warps and 8 blocks, each off by 2^-23 of what is summed (matrix sums cut off).
