@@ -1192,7 +1192,7 @@ cudaError_t launch_kv_attention(KvAttnArgs a, cudaStream_t st) {
   });
   if (setup_err[dev] != cudaSuccess) return setup_err[dev];
   const int R = 8 * NT;
-  const long long rt = ((long long)a.d.max_new * a.d.G + R - 1) / R;
+  const long long rt = ((long long)std::min(a.d.max_new, a.d.n_new) * a.d.G + R - 1) / R;
   const long long units = rt * a.d.B * a.d.Hkv;
   a.split = kv_split(a.d) ? 1 : 0;
   const long long blocks = a.split ? units * ((a.d.max_len + kBlk - 1) / kBlk) : units;
@@ -1219,8 +1219,8 @@ template <int HD, int NH>
 cudaError_t launch_kv_append_n(AppendArgs a, int rope, cudaStream_t st) {
   a.heads = (a.d.Hkv + NH - 1) / NH;
   a.roles = 2 * a.heads + (a.q_out ? (a.d.H + kQueryHeads - 1) / kQueryHeads : 0);
-  // a sequence's max_new tokens touch at most so many blocks
-  const dim3 grid(((a.d.max_new + kBlk - 2) / kBlk + 1) * a.roles, a.d.B);
+  // a sequence's new tokens touch at most so many blocks
+  const dim3 grid(((std::min(a.d.max_new, a.d.n_new) + kBlk - 2) / kBlk + 1) * a.roles, a.d.B);
   launch_begin(KID_KV_APPEND, st);
   const cudaError_t e = launch_after(rope == MMDIT_ROPE_NONE    ? kv_append_kernel<HD, NH, MMDIT_ROPE_NONE>
                                      : rope == MMDIT_ROPE_PAIRS ? kv_append_kernel<HD, NH, MMDIT_ROPE_PAIRS>

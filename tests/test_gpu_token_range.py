@@ -7,7 +7,7 @@ import torch
 
 from diffusion_transformer_image_mmdit_gb300 import api
 from tests import token_oracle as T
-from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn, w4_case,
+from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn, tables, w4_case,
                                       within)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -136,6 +136,28 @@ def test_kv_attention_bounds_far_above_the_lengths():
     for o in outs[1:]:
         assert float((o - outs[0]).abs().max()) <= 2.0 ** -6 * float(outs[0].abs().max())
     assert max(took[1:]) <= 4 * took[0] + 300, took
+
+
+def test_kv_append_bounds_far_above_the_rows():
+    """Three rows under a bound of 2^20 new tokens: the cache of the tight bound, and about its time (no sequence has more
+    new tokens than there are rows; a factor of 4 and 300 us are left for the launches)."""
+    g = gen(66)
+    sq = Seqs(g, [300, 5, 64], [1, 1, 1])
+    tokens = random_cache(g, sq.n_blocks, 8, 64)
+    qkv = randn(g, 3, 48 * 64).to(BF16).cuda()
+    cos, sin = tables(400, 64)
+    cos, sin = (torch.nn.functional.pad(t, (0, 0, 0, 2 ** 20 - 400)) for t in (cos, sin))
+    took, got = [], []
+    for max_new in (1, 2 ** 20):
+        cache = device_cache(*tokens, sq)
+        wide = api.KVCacheDev(cache.k, cache.v, cache.k_scale, cache.v_scale,
+                              torch.nn.functional.pad(cache.table, (0, 2 ** 14 - cache.table.shape[1])), cache.len, cache.start)
+        shape = sq.shape(32, 8, 64, max_new=max_new, max_len=2 ** 20, table_ld=2 ** 14)
+        q = torch.empty(3, 32 * 64, dtype=BF16, device="cuda")
+        took.append(device_us(lambda: api.mmdit_kv_append(shape, wide, qkv, cos, sin, q)))
+        got.append((q, cache.k, cache.v, cache.k_scale, cache.v_scale))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert took[1] <= 4 * took[0] + 300, took
 
 
 # ------------------------------------------------------------------ 4-bit products
