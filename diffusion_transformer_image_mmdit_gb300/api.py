@@ -567,8 +567,9 @@ def make_kv_shape(B, H, H_kv, d_head, n_blocks, table_ld, n_new, max_new, max_le
 class KVCacheDev:
     """A paged e4m3 key/value cache and the sequences of a call (mmdit_kv_cache_t): codes k uint8
     [n_blocks, H_kv, 64, d], v uint8 [n_blocks, H_kv, d, 64], scales fp32 [n_blocks, H_kv], the block table int32
-    [B, table_ld], lengths int32 [B] (new tokens included) and first rows int32 [B + 1].  The tensors are checked once,
-    here.  The three index tensors may be rewritten in place between calls; other tensors make another KVCacheDev."""
+    [B, entries] (rows may be strided: table_ld is its row stride), lengths int32 [B] (new tokens included) and first
+    rows int32 [B + 1].  The tensors are checked once, here.  The three index tensors may be rewritten in place between
+    calls; other tensors make another KVCacheDev."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -582,24 +583,33 @@ class KVCacheDev:
         B = self.len.shape[0]
         if blk != MMDIT_KV_BLOCK or self.table.dim() != 2:
             raise ValueError("k: [n_blocks, H_kv, 64, d_head]; table: [B, table_ld]")
-        dev, ld = _device(self.k), self.table.shape[1]
+        dev, table = _device(self.k), self.table
+        entries, ld = table.shape[1], max(table.stride(0), table.shape[1] if B == 1 else 0)
+        if table.dtype is not torch.int32 or table.shape[0] != B or table.get_device() != dev or ld < entries or (
+                table.stride(1) != 1 and entries > 1):
+            raise ValueError(f"table: expected int32 rows [{B}, entries] on cuda:{dev}, each contiguous, none on another; "
+                             f"got {table.dtype} {tuple(table.shape)} with strides {table.stride()} on {table.device}")
         struct = KVCache(_tensor("k", self.k, torch.uint8, (n, h, blk, d), dev),
                          _tensor("v", self.v, torch.uint8, (n, h, d, blk), dev),
                          _tensor("k_scale", self.k_scale, torch.float32, (n, h), dev),
                          _tensor("v_scale", self.v_scale, torch.float32, (n, h), dev),
-                         _tensor("table", self.table, torch.int32, (B, ld), dev),
+                         table.data_ptr(),
                          _tensor("len", self.len, torch.int32, (B,), dev),
                          _tensor("start", self.start, torch.int32, (B + 1,), dev))
         object.__setattr__(self, "_struct", struct)
-        object.__setattr__(self, "_dims", (n, h, d, B, ld))
+        object.__setattr__(self, "_dims", (n, h, d, B))
+        object.__setattr__(self, "_table", (ld, entries if B == 1 else ld, entries * MMDIT_KV_BLOCK))
         object.__setattr__(self, "_dev", dev)
 
     def struct(self) -> KVCache:
         return self._struct
 
     def _fits(self, s: KVShape) -> int:
-        if self._dims != (s.n_blocks, s.H_kv, s.d_head, s.B, s.table_ld):
+        ld, one, most = self._table  # one row may be called as long as it is
+        if self._dims != (s.n_blocks, s.H_kv, s.d_head, s.B) or s.table_ld != ld and s.table_ld != one:
             raise ValueError("the cache's tensors do not have the shape's sizes")
+        if s.max_len > most:
+            raise ValueError(f"max_len {s.max_len}: the table's rows hold the blocks of {most} tokens")
         if self._dev != torch.cuda.current_device():
             raise ValueError(f"the cache's device cuda:{self._dev} must be the current CUDA device")
         return self._dev

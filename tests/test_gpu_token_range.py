@@ -7,8 +7,8 @@ import torch
 
 from diffusion_transformer_image_mmdit_gb300 import api
 from tests import token_oracle as T
-from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn, tables, w4_case,
-                                      within)  # noqa: F401
+from tests.test_gpu_token_ops import (BF16, F64, Seqs, _gpu, device_cache, gen, random_cache, randn, run_attention,
+                                      tables, w4_case, within)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +246,29 @@ def test_gemv_w4_infinities():
     assert torch.equal(torch.isnan(y), torch.isnan(ref))
     inf = torch.isinf(ref)
     assert torch.equal(torch.isinf(y), inf) and torch.equal(y[inf], ref[inf])
+
+
+# ------------------------------------------------------------------ handles
+def test_kv_cache_takes_a_slice_of_a_wider_table():
+    """The block table of a batch may be rows of a wider one; a bound beyond its columns is refused."""
+    g = gen(72)
+    sq = Seqs(g, [700, 90, 3], [1, 2, 1], extra_entries=0)
+    shape, cache, q, out, _ = run_attention(g, sq, 4, 2, 64, rows_behind=0)
+    wide = torch.full((3, 40), -5, dtype=torch.int32, device="cuda")
+    wide[:, 4:4 + sq.table_ld] = cache.table
+    part = api.KVCacheDev(cache.k, cache.v, cache.k_scale, cache.v_scale, wide[:, 4:4 + sq.table_ld], cache.len, cache.start)
+    got = attend(sq.shape(4, 2, 64, table_ld=40), part, q)
+    assert torch.equal(got, out.cpu())
+    # one sequence of it, under either row length
+    one = api.KVCacheDev(cache.k, cache.v, cache.k_scale, cache.v_scale, wide[:1, 4:4 + sq.table_ld], cache.len[:1].clone(),
+                         cache.start[:2].clone())
+    for ld in (40, sq.table_ld):
+        got = attend(sq.shape(4, 2, 64, B=1, n_new=1, max_new=1, table_ld=ld), one, q[:1]).float()
+        # another batch is cut in other places, and rounds differently
+        assert float((got - out[:1].cpu().float()).abs().max()) <= 2.0 ** -6 * float(got.abs().max())
+    with pytest.raises(ValueError):
+        attend(sq.shape(4, 2, 64, table_ld=40, max_len=sq.table_ld * 64 + 1), part, q)
+    with pytest.raises(ValueError):
+        attend(shape, part, q)  # the table's own stride
+    with pytest.raises(ValueError):
+        api.KVCacheDev(cache.k, cache.v, cache.k_scale, cache.v_scale, wide.t()[:3], cache.len, cache.start)
