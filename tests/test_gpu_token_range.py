@@ -101,6 +101,12 @@ def test_kv_attention_query_channel_that_meets_zero_keys(d):
     within(out.view(2, d), o, tol, "outlier channel")
 
 
+def test_kv_attention_of_a_prompt():
+    """Prompts of hundreds of new tokens, alone and behind older ones, units whole and cut."""
+    run_attention(gen(61), Seqs(gen(62), [0, 130], [515, 300]), 4, 2, 128)
+    run_attention(gen(63), Seqs(gen(64), [0], [400]), 6, 2, 64)
+
+
 def device_us(f, n=5):
     f()
     best = math.inf
