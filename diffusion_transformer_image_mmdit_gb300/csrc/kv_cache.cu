@@ -171,21 +171,20 @@ __device__ __forceinline__ uint32_t move_codes(uint32_t w, float factor) {
 }
 
 // Blocks of 256 threads, of three kinds, per touched cache block and sequence;
-// all kinds of one cache block lie side by side in the grid, so that the parts
-// of a row are read at about the same time (115 us against 112.5 with one kind
-// after the other, at 24 prompts).
+// all kinds of one cache block lie side by side in the grid (24 prompts 94.9 us,
+// one token 3.5; one kind after the other 93.9 and 3.6).
 //   keys of NH kv heads: rotates them, finds their maxima, sets the scales
 //     (moving the codes that are there if a scale grows) and writes the codes;
 //   values of NH kv heads: the same without a rotation, transposed through
 //     shared memory, so that whole words of a channel are written;
 //   queries of kQueryHeads heads: rotates them, the next heads' loads in flight
-//     while one batch is turned, on one position's cosines and sines (8 heads are
-//     no faster, 2 take 141 us for 115).
+//     while one batch is turned, on one position's cosines and sines (2 or 8
+//     heads per block take 108 us for 95).
 // Keys and values wait in registers as they came between the maximum and the
 // codes.  Bound by the read of the rows and the write of queries and codes, and
 // by having enough loads in flight: 64 registers leave four blocks on an SM
-// (three blocks of 80: 111 us).  24 prompts of 77 to 2048 tokens (32 query, 8 kv
-// heads of 128) move 575 MB in 96 us, 6.0 TB/s, 0.88 of the copy bandwidth; one
+// (three blocks of 80: 104 us).  24 prompts of 77 to 2048 tokens (32 query, 8 kv
+// heads of 128) move 575 MB in 95 us, 6.1 TB/s, 0.89 of the copy bandwidth; one
 // token of one sequence takes 3.5 us, three loads one behind the other.
 template <int HD, int NH, int ROPE>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
@@ -470,17 +469,29 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
 // slots were slower: 48 sequences 73.5 us for 70.5, one long 59.7 for 55.0).
 // Measured with 32 query and 8 kv heads of 128: one token of 48 sequences of 33
 // to 8192 70 us (405 MB, 5.8 TB/s, 0.85 of the copy bandwidth), three tokens of
-// one sequence of 131069 51.4 us (5.2 TB/s, 0.77: of twice the length the second
+// one sequence of 131069 51.9 us (5.2 TB/s, 0.76: of twice the length the second
 // half takes 40 us, the copy bandwidth; 12 us are the way to the first block, the
-// SMs that are slower than others, and the merge), one token behind 511 6.6 us,
-// six loads and two launches one behind the other.
+// SMs that are slower than others, and the merge), one token behind 511 6.7 us in
+// one launch of 8 blocks: six loads one behind the other, then two items of keys
+// and of values per warp, and the merge of the warps.
+//
+// Prompts are right but not fast here: every 16 rows of a kv head read and widen
+// the cache anew, and every such tile is a unit with its fixed cost (one prompt of
+// 512 43.6 us, of 2048 330; 24 of 77 to 2048 2.85 ms).
 constexpr int kKvMaxCtas = 320;
 constexpr int kKvWarps = 4;
 constexpr int kKvRing = 24576;      // bytes of a warp's ring
 constexpr int kKvCtaMinBlocks = 4;  // least blocks per thread block when units are cut
-constexpr int kKvWholeBlocks = 8;   // units of up to so many blocks are not cut (no workspace, one launch)
-constexpr int kKvUnitCost = 10;     // what a unit costs beside its blocks (queries, merge), in blocks: 48
-                                    // sequences of 33 to 8192 took 84 us with 0, 77 with 4, 71 with 6 and 13, 70 with 10
+// Units of up to so many blocks are not cut (no workspace, one launch).  One token
+// each of 1, 4 and 16 sequences, us, whole and cut: of 512 tokens 6.6, 6.9, 7.2 and
+// 6.9, 7.8, 10.0; of 1024 tokens 9.3, 9.6, 10.4 and 6.9, 8.0, 12.3; of 2048 tokens
+// 14.9, 15.2, 16.6 and 7.0, 11.1, 19.0.
+constexpr int kKvWholeBlocks = 8;
+// What a unit costs beside its blocks (queries, merge), in blocks.  With 0, 4, 10
+// and 16, us: 48 sequences of 33 to 8192 tokens 88.7, 73.7, 70.3, 70.9; 16 of 2000
+// to 6000 30.2, 29.5, 28.5, 29.2; 200 of 100 to 1500 98.8, 71.4, 64.2, 65.7; one of
+// 60000 and 40 of 300 48.9, 39.2, 32.3, 32.4.
+constexpr int kKvUnitCost = 10;
 
 struct KvAttnArgs {
   KvDims d;
@@ -1061,7 +1072,7 @@ __global__ void __launch_bounds__(128, 2) kv_attention_kernel(const KvAttnArgs a
 // grid's x dimension goes over the units or, where fewer (as with many tokens,
 // or bounds above the lengths: units are numbered by the shape's bounds), over
 // the boundaries between the attention's blocks: a unit that is cut is merged by
-// the first boundary inside it.  Few registers (32 per thread; 51 with 16
+// the first boundary inside it.  Few registers (48 per thread; 40 with 16
 // warps): blocks come on an SM beside one of the attention's, and find their
 // unit while others still read.
 template <int HD, int NT, int W>
@@ -1205,7 +1216,7 @@ cudaError_t launch_kv_attention(KvAttnArgs a, cudaStream_t st) {
   const int by_unit = units < grid;
   const dim3 rows((unsigned)(by_unit ? units : std::max(1, grid - 1)),
                   (unsigned)std::min<long long>(R, (long long)a.d.max_new * a.d.G));
-  // Few rows to merge have many parts each.  One sequence of 131069 takes 51.4
+  // Few rows to merge have many parts each.  One sequence of 131069 took 51.4
   // us with 16 warps a row, 53 with 8, 54.3 with 4, 57.4 with 2; 48 sequences
   // 81.8, 73.1, 70.0 and 70.1; 8 sequences 28.5 with 16, 28.8 with 4.
   const bool few = (long long)rows.x * rows.y <= 2 * num_sms();

@@ -476,11 +476,11 @@ int mmdit_time_embed(const mmdit_shape_t* shape, const mmdit_linear_t* time1, co
  * y = h / sqrt(mean(h^2) + eps) * gain, in fp32.
  * x: device [rows, D], row stride x_ld, x_dtype MMDIT_F32 or MMDIT_BF16;
  * delta: device [rows, D], row stride delta_ld, delta_dtype likewise, or NULL
- * (h = x).  x_out: device, x's type and row stride, gets h rounded once; NULL,
- * or x itself for the update in place (no other overlap).  gain: device fp32
- * [D].  Outputs, one at least: y device bf16 [rows, D]; q device e4m3 bytes
- * [rows, D] with s device fp32 [rows], s = max|y| / 448 (1 for a zero row,
- * 2^-126 at least) and q = e4m3(y / s) of the fp32 values of y
+ * (h = x; x_out is NULL then).  x_out: device, x's type and row stride, gets h
+ * rounded once; NULL, or x itself for the update in place (no other overlap).
+ * gain: device fp32 [D].  Outputs, one at least: y device bf16 [rows, D]; q
+ * device e4m3 bytes [rows, D] with s device fp32 [rows], s = max|y| / 448 (1 for
+ * a zero row, 2^-126 at least) and q = e4m3(y / s) of the fp32 values of y
  * (mmdit_linear_f8_fwd's operand).  No output but x_out overlaps an input.
  * D a multiple of 8, D <= 32768; row strides multiples of 8, >= D.  rows = 0
  * does nothing.  A row with an infinity or a NaN has no defined q and s. */
@@ -527,12 +527,12 @@ int mmdit_gemv_w4(const mmdit_linear_w4_t* lin, int B, int N, int K, const void*
 #define MMDIT_ROPE_HALVES 2 /* channels i and i + d_head / 2 turn together */
 typedef struct {
   int B;         /* sequences, <= 65535 */
-  int H;         /* query heads, a multiple of H_kv; query heads h (H / H_kv) .. share kv head h */
+  int H;         /* query heads, a multiple of H_kv, <= 65536; query heads h (H / H_kv) .. share kv head h */
   int H_kv;      /* key / value heads, <= 32767 */
   int d_head;    /* 64 or 128 */
   int n_blocks;  /* blocks in the cache */
-  int table_ld;  /* entries of the block table per sequence, table_ld * MMDIT_KV_BLOCK >= max_len */
-  int n_new;     /* rows of new tokens, all sequences together */
+  int table_ld;  /* row stride of the block table in entries, table_ld * MMDIT_KV_BLOCK >= max_len */
+  int n_new;     /* rows of new tokens, all sequences together, <= 2^28 */
   int max_new;   /* a bound on the new tokens of one sequence; max_new (H / H_kv) = r <= 2^30, ceil(r / 8) B H_kv too */
   int max_len;   /* a bound on the tokens of one sequence, new ones included, <= 2^28 */
   int rope;      /* MMDIT_ROPE_* */
