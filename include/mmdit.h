@@ -592,9 +592,10 @@ int mmdit_kv_append(const mmdit_kv_shape_t* shape, const mmdit_kv_cache_t* cache
  * q, out: device bf16 [n_new, H * d_head], no overlap.  ws: device workspace of
  * mmdit_kv_workspace_size(shape) bytes, used by one call at a time (calls that
  * can overlap need one each).  Sums are added up in a fixed order: the same
- * call gives the same bits.  Scores, softmax statistics and sums in fp32; a
- * probability meets the values as f16, off by at most 2^-11 of itself, or
- * 2^-39 of the largest one where that is more. */
+ * call gives the same bits.  Scores, softmax statistics and sums in fp32 (for
+ * scale * max|q| * k_scale up to 2^108); a probability meets the values as f16,
+ * off by at most 2^-11 of itself, or 2^-39 of the largest one where that is
+ * more. */
 int mmdit_kv_workspace_size(const mmdit_kv_shape_t* shape, size_t* bytes);
 int mmdit_kv_attention(const mmdit_kv_shape_t* shape, const mmdit_kv_cache_t* cache, const void* q, void* out, void* ws,
                        size_t ws_bytes, void* stream);
